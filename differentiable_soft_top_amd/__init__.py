@@ -20,11 +20,11 @@ from ._lib import Params, SoftTopKError, Stats  # noqa: F401
 
 from .experts import (  # noqa: F401
     Dispatch, combine, combine_backward, combine_forward, dispatch, experts_backward, experts_forward,
-    experts_product, moe, route, route_backward, route_forward)
+    experts_product, experts_residual_backward, moe, route, route_backward, route_forward)
 
 __all__ = ["soft_topk", "forward", "backward", "rows_forward", "rows_backward", "threshold_curve", "dftopk_forward",
            "route", "route_forward", "route_backward", "Dispatch", "dispatch", "experts_product", "experts_forward",
-           "experts_backward", "combine", "combine_forward", "combine_backward", "moe",
+           "experts_backward", "experts_residual_backward", "combine", "combine_forward", "combine_backward", "moe",
            "Params", "Stats", "SoftTopKError", "default_params"]
 
 

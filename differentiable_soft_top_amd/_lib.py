@@ -134,6 +134,8 @@ def load():
     lib.soft_topk_experts_backward.restype = ctypes.c_int
     lib.soft_topk_experts_backward_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32]
     lib.soft_topk_experts_backward_workspace_bytes.restype = sz
+    lib.soft_topk_experts_residual_backward.argtypes = [vp, i32, vp, i64, i32, i32, vp, vp]
+    lib.soft_topk_experts_residual_backward.restype = ctypes.c_int
     lib.soft_topk_combine_forward.argtypes = [vp, fp, vp, vp, i32, i64, i32, i64, i32, vp, vp]
     lib.soft_topk_combine_forward.restype = ctypes.c_int
     lib.soft_topk_combine_backward.argtypes = [vp, vp, fp, vp, i32, i64, i32, i64, i32, vp, fp, vp, sz, vp]

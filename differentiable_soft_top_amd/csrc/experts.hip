@@ -934,6 +934,44 @@ __global__ __launch_bounds__(kBiasWaves* kWave) void experts_bias_kernel(Experts
     reinterpret_cast<typename T::Store*>(a.db)[(int64_t)e * a.M + n] = T::down(s);
 }
 
+// The residual's gradient: dy before the last row of the last expert, 0 from
+// there on (y is 0 there whatever the residual holds).  kWhole: both are
+// aligned 16-byte pieces.  Bound by memory.
+constexpr int kResidualBlocks = 2048;
+constexpr int kResidualLoads = 4;  // pieces of a thread in flight
+
+template <bool kWhole>
+__global__ __launch_bounds__(256) void experts_residual_kernel(ExpertsArgs a, uint16_t* dr)
+{
+    const uint16_t* const dy = reinterpret_cast<const uint16_t*>(a.dy);
+    const int64_t n = (int64_t)a.pairs * a.N, kept = (int64_t)clamp_row(a.offsets[a.experts], a.pairs) * a.N;
+    constexpr int64_t kApart = 256 * 8;  // elements between a thread's pieces
+    for (int64_t first = (int64_t)blockIdx.x * (kApart * kResidualLoads); first < n;
+         first += (int64_t)gridDim.x * (kApart * kResidualLoads)) {
+        const int64_t at = first + threadIdx.x * 8;
+        if (kWhole && first + kApart * kResidualLoads <= kept) {
+            V4U u[kResidualLoads];
+#pragma unroll
+            for (int i = 0; i < kResidualLoads; ++i)
+                u[i] = __builtin_nontemporal_load(reinterpret_cast<const V4U*>(dy + at + i * kApart));
+#pragma unroll
+            for (int i = 0; i < kResidualLoads; ++i)
+                __builtin_nontemporal_store(u[i], reinterpret_cast<V4U*>(dr + at + i * kApart));
+        } else if (kWhole && first >= kept && first + kApart * kResidualLoads <= n) {
+#pragma unroll
+            for (int i = 0; i < kResidualLoads; ++i)
+                __builtin_nontemporal_store(V4U{0u, 0u, 0u, 0u}, reinterpret_cast<V4U*>(dr + at + i * kApart));
+        } else {
+#pragma unroll 8
+            for (int j = 0; j < 8 * kResidualLoads; ++j) {
+                const int64_t e = first + j * 256 + threadIdx.x;
+                if (e < n)
+                    dr[e] = e < kept ? dy[e] : (uint16_t)0;
+            }
+        }
+    }
+}
+
 // dx of every place: dz (rows) times W_e (its columns), summed over M.
 // 8192^3 776 us, 1417 TFLOP/s; 65,536 rows of 64 uneven experts, 2048 to 2048,
 // 640 us: its row tiles are 12% part-filled, 32 steps leave a tile's start and
@@ -1383,6 +1421,18 @@ int32_t experts_bias_tiles(int64_t pairs, int32_t experts)
 hipError_t launch_experts_forward(const ExpertsArgs& a, int dtype, hipStream_t stream)
 {
     return dtype == SOFT_TOPK_BF16 ? forward<Bf16>(a, stream) : forward<F16>(a, stream);
+}
+
+hipError_t launch_experts_residual(const ExpertsArgs& a, void* dr, hipStream_t stream)
+{
+    const bool whole = ((reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(dr)) & 15) == 0;
+    uint16_t* const to = static_cast<uint16_t*>(dr);
+    const dim3 grid(kResidualBlocks), block(256);
+    if (whole)
+        STK_LAUNCH(kKExpertsBackward, stream, (experts_residual_kernel<true>), grid, block, 0, stream, a, to);
+    else
+        STK_LAUNCH(kKExpertsBackward, stream, (experts_residual_kernel<false>), grid, block, 0, stream, a, to);
+    return hipGetLastError();
 }
 
 hipError_t launch_experts_backward(const ExpertsArgs& a, int dtype, hipStream_t stream)

@@ -236,6 +236,22 @@ int soft_topk_experts_backward(const void* grad_y, const void* x, const void* w,
     return done(launch_experts_backward(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
+int soft_topk_experts_residual_backward(const void* grad_y, int32_t dtype, const int32_t* offsets, int64_t pairs,
+                                        int32_t experts, int32_t N, void* grad_residual, void* stream)
+{
+    if (!grad_y || !offsets || !grad_residual || !half_type(dtype) || !in_range(pairs) || !experts_ok(experts) ||
+        N < 1 || !aligned(grad_y, 2) || !aligned(grad_residual, 2))
+        return SOFT_TOPK_EINVAL;
+    ExpertsArgs a;
+    memset(&a, 0, sizeof(a));
+    a.pairs = (int32_t)pairs;
+    a.experts = experts;
+    a.N = N;
+    a.offsets = offsets;
+    a.dy = grad_y;
+    return done(launch_experts_residual(a, grad_residual, static_cast<hipStream_t>(stream)));
+}
+
 int soft_topk_combine_forward(const void* y, const float* weights, const int32_t* slots, const void* residual,
                               int32_t dtype, int64_t tokens, int32_t k, int64_t places, int32_t N, void* out,
                               void* stream)

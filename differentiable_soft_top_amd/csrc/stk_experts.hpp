@@ -94,6 +94,7 @@ struct ExpertsArgs {
 };
 hipError_t launch_experts_forward(const ExpertsArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_experts_backward(const ExpertsArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_experts_residual(const ExpertsArgs& a, void* dr, hipStream_t stream);  // dr: like y
 int32_t experts_bias_tiles(int64_t pairs, int32_t experts);  // rows of dbp
 int32_t experts_weight_shares(int64_t pairs, int32_t experts, int32_t K, int32_t M);  // of dwp, 1: none
 

@@ -168,6 +168,17 @@ def _experts_backward(grad_y, x, w, offsets, rows, slots, z, act, k, want):
     return dx, dw, db
 
 
+def _residual_backward(grad_y, offsets):
+    pairs, N = grad_y.shape
+    g = _torch.empty_like(grad_y)
+    rc = _lib.load().soft_topk_experts_residual_backward(grad_y.data_ptr(), _TYPES[grad_y.dtype], offsets.data_ptr(),
+                                                         pairs, offsets.shape[0] - 1, N, g.data_ptr(),
+                                                         _stream(grad_y.device))
+    if rc:
+        _lib.check(rc, "soft_topk_experts_residual_backward")
+    return g
+
+
 def _combine_backward(grad_out, y, weights, slots, want):
     torch = _torch
     T, k = slots.shape
@@ -282,6 +293,15 @@ def experts_backward(grad_y, x, w, plan: Dispatch, z=None, act: str = "none", wa
                                  ACTS[act], k, want)
 
 
+def experts_residual_backward(grad_y, plan: Dispatch):
+    """soft_topk_experts_residual_backward: the residual's gradient, grad_y with 0 behind the last row."""
+    _load()
+    _check(grad_y, "grad_y", _HALVES, 2)
+    _check(plan.offsets, "offsets", _INT32, 1, grad_y.device)
+    with _on(grad_y.device):
+        return _residual_backward(grad_y, plan.offsets)
+
+
 def _combine_sizes(y, weights, slots, residual):
     torch = _torch
     _check(y, "y", _FLOATS, 2)
@@ -361,12 +381,16 @@ def _functions():
 
     def product_grad(ctx, gy):
         want = ctx.needs_input_grad
-        dx = dw = db = None
-        if gy is not None and (want[0] or want[1] or want[2]):
+        dx = dw = db = dr = None
+        if gy is not None:
             x, w, z, offsets, rows, slots = ctx.saved_tensors
-            k = slots.shape[1] if rows is not None and slots is not None else 1
-            dx, dw, db = _experts_backward(gy.contiguous(), x, w, offsets, rows, slots, z, ctx.act, k, want)
-        return dx, dw, db, gy if want[3] else None, None, None, None, None
+            gy = gy.contiguous()
+            if want[0] or want[1] or want[2]:
+                k = slots.shape[1] if rows is not None and slots is not None else 1
+                dx, dw, db = _experts_backward(gy, x, w, offsets, rows, slots, z, ctx.act, k, want)
+            if want[3]:
+                dr = _residual_backward(gy, offsets)
+        return dx, dw, db, dr, None, None, None, None
 
     class _Product(torch.autograd.Function):
         @staticmethod

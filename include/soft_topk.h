@@ -475,7 +475,8 @@ int soft_topk_experts_forward(const void* x, const void* w, const void* bias, co
                               void* stream);
 
 /*
- * Gradients of soft_topk_experts_forward (the residual's is grad_y itself).
+ * Gradients of soft_topk_experts_forward (the residual's:
+ * soft_topk_experts_residual_backward).
  * z: the forward's out_z (may be NULL for SOFT_TOPK_ACT_NONE).  slots:
  * int32[tokens][k] as soft_topk_dispatch writes them, needed for grad_x when
  * rows is given (pairs = tokens * k).  grad_x, grad_w, grad_bias: like x, w,
@@ -493,6 +494,16 @@ int soft_topk_experts_backward(const void* grad_y, const void* x, const void* w,
                                void* stream);
 size_t soft_topk_experts_backward_workspace_bytes(int64_t pairs, int32_t experts, int32_t K, int32_t N, int32_t act,
                                                   int32_t has_rows);
+
+/*
+ * Gradient of soft_topk_experts_forward's residual: grad_y before row
+ * offsets[experts] (taken within [0, pairs]) and 0 from it on, where y is 0
+ * whatever the residual holds.  grad_y, grad_residual: [pairs][N] of `dtype`
+ * (bf16 or fp16), not overlapping.  No workspace; asynchronous on `stream`.
+ * Errors: EINVAL before any launch; EHIP.
+ */
+int soft_topk_experts_residual_backward(const void* grad_y, int32_t dtype, const int32_t* offsets, int64_t pairs,
+                                        int32_t experts, int32_t N, void* grad_residual, void* stream);
 
 /*
  * Weighted sum back to the tokens: out_t = residual_t + sum_j w_tj

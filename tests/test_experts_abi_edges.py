@@ -1,0 +1,32 @@
+"""Host-side checks of the expert operators' edges (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from differentiable_soft_top_amd import _lib
+
+FAKE = ctypes.c_void_p(0x100000)
+ODD = ctypes.c_void_p(0x100001)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def test_residual_refusals(lib):
+    def call(dy=FAKE, dtype=1, off=FAKE, R=20, E=4, N=8, dr=FAKE):
+        return lib.soft_topk_experts_residual_backward(dy, dtype, off, R, E, N, dr, None)
+
+    for bad in (dict(dy=None), dict(off=None), dict(dr=None), dict(dtype=0), dict(dtype=3), dict(R=0), dict(R=-1),
+                dict(R=1 << 31), dict(E=0), dict(E=1025), dict(N=0), dict(dy=ODD), dict(dr=ODD)):
+        assert call(**bad) == _lib.EINVAL, bad
+
+
+def test_residual_refuses_host_tensors():
+    import torch
+
+    import differentiable_soft_top_amd as stk
+
+    with pytest.raises(TypeError):
+        stk.experts_residual_backward(torch.zeros(4, 2).half(), stk.Dispatch(torch.zeros(2, dtype=torch.int32)))

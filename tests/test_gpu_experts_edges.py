@@ -1,0 +1,117 @@
+"""GPU tests of the expert operators where a call is easily answered wrongly: rows that no expert holds, scores whose
+parts cancel or leave the fp32 range, tails of an activation, router rows that are not finite, offsets that fall, and
+sizes near what a launch can hold.  The plain fp64 references and their bounds are those of experts_reference.py."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import experts_reference as ref  # noqa: E402
+import test_gpu_experts as base  # noqa: E402
+
+import differentiable_soft_top_amd as stk  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+gen, within = base.gen, base.within
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm device")
+    return torch.device("cuda:0")
+
+
+# ---- the residual's gradient behind the last row -----------------------------
+
+RESIDUALS = [p for p in base.PRODUCTS if p[8] and p[10] > 0.0]
+
+
+def residual_gradient(dy, offsets):
+    """y_r = act(z_r) + residual_r before offsets[E], 0 behind: dy there, 0 behind."""
+    want = dy.clone()
+    want[int(offsets[-1]):] = 0
+    return want
+
+
+@pytest.mark.parametrize("T,k,E,K,N,act,dtype,bias,residual,gather,dropped", RESIDUALS)
+@pytest.mark.parametrize("odd", [False, True])
+def test_product_residual_with_dropped_pairs(dev, T, k, E, K, N, act, dtype, bias, residual, gather, dropped, odd):
+    print("[residual] T=%d K=%d N=%d odd=%d" % (T, K, N, odd), flush=True)
+    x, w, offsets, rows, slots, b, res, dy = base.product_inputs(T, k, E, K, N, act, dtype, bias, residual, gather,
+                                                                 dropped)
+    total = int(offsets[-1])
+    assert total < T * k
+    dy[total:] = math.nan  # reaches nothing
+    plan = stk.Dispatch(*(None if t is None else t.to(dev) for t in (offsets, rows, slots)))
+    leaves = [base.place(t, dev, odd) for t in (x, w, b, res)]
+    leaves = [None if t is None else t.requires_grad_(True) for t in leaves]
+    y = stk.experts_product(leaves[0], leaves[1], plan, bias=leaves[2], act=act, residual=leaves[3])
+    given = [t for t in leaves if t is not None]
+    grads = torch.autograd.grad(y, given, base.place(dy, dev, odd))
+    want = ref.product(x, w, offsets, rows, b, act, res, dy)
+    for got, (value, bound), what in zip((y,) + grads, want, ("y", "dx", "dw", "db")[:len(given)]):
+        within(got, value, bound, what)
+    assert torch.equal(grads[-1].cpu(), residual_gradient(dy, offsets))
+    assert torch.equal(stk.experts_residual_backward(base.place(dy, dev, odd), plan), grads[-1])
+
+
+def test_product_residual_by_differences(dev):
+    # moving the residual behind the last row moves nothing
+    x, w, offsets, rows, slots, b, res, dy = base.product_inputs(40, 2, 5, 64, 24, "silu", "bf16", True, True, True, 0.4)
+    plan = stk.Dispatch(offsets.to(dev), rows.to(dev), slots.to(dev))
+    total = int(offsets[-1])
+    leaf = res.to(dev).requires_grad_(True)
+
+    def loss(r):
+        y = stk.experts_product(x.to(dev), w.to(dev), plan, bias=b.to(dev), act="silu", residual=r)
+        return (y.double() * dy.to(dev).double()).sum()
+
+    with torch.no_grad():
+        moved = leaf.clone()
+        moved[total:] += 1
+        assert float(loss(moved)) == float(loss(leaf))
+    (grad,) = torch.autograd.grad(loss(leaf), [leaf])
+    assert torch.equal(grad.cpu(), residual_gradient(dy, offsets))
+
+
+@pytest.mark.parametrize("kept", [0, 1, 333])
+def test_residual_gradient_of_none_and_all_rows(dev, kept):
+    # alone (x, w and bias need no gradient), from a sum: a gradient without storage of its own
+    N = 37
+    offsets = torch.tensor([0, 0, kept], dtype=torch.int32)
+    x, w = torch.randn(333, 16, generator=gen(1)).half(), torch.randn(2, N, 16, generator=gen(2)).half()
+    res = torch.zeros(333, N, dtype=torch.float16, device=dev, requires_grad=True)
+    y = stk.experts_product(x.to(dev), w.to(dev), stk.Dispatch(offsets.to(dev)), residual=res)
+    (grad,) = torch.autograd.grad(y.sum(), [res])
+    want = torch.zeros(333, N, dtype=torch.float16)
+    want[:kept] = 1
+    assert torch.equal(grad.cpu(), want)
+
+
+def test_residual_gradient_behind_4_gib(dev):
+    P, N = 1_100_000, 2048
+    kept = P - 3
+    dy = torch.ones(P, N, dtype=torch.bfloat16, device=dev)
+    plan = stk.Dispatch(torch.tensor([0, 5, kept], dtype=torch.int32, device=dev))
+    grad = stk.experts_residual_backward(dy, plan)
+    assert (grad[kept:] == 0).all() and (grad[:kept] == 1).all()
+
+
+def test_residual_gradient_captured_and_replayed(dev):
+    dy = torch.randn(500, 72, generator=gen(3)).to(torch.bfloat16).to(dev)
+    offsets = torch.tensor([0, 100, 500], dtype=torch.int32, device=dev)
+    plan = stk.Dispatch(offsets)
+    stk.experts_residual_backward(dy, plan)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = stk.experts_residual_backward(dy, plan)
+    for kept in (500, 0, 123, 499):
+        offsets[2] = kept
+        want = stk.experts_residual_backward(dy, plan)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(out.cpu(), residual_gradient(dy.cpu(), [kept]))
