@@ -424,16 +424,13 @@ __global__ __launch_bounds__(kRouteWaves* kWave, kPlain ? 6 : 4) void route_forw
     const float top = row_max<G>(mine);
     bad |= top == INFINITY;
     double total = 0.0;
-    if (!kPlain && softmax && a.bias) {  // u needs it in fp64
+    // The weights or u need it: in fp64, so that a weight is rounded once and
+    // agrees with the gradient's p (65,536 x 256 bf16: 40 us, with fp32
+    // exponentials 29).
+    if (softmax && (!a.renorm || (!kPlain && a.bias))) {
 #pragma unroll 4
         for (int r = 0; r < R; ++r)
             total += z[r] > -INFINITY ? exp64((double)z[r] - (double)top) : 0.0;
-        total = row_sum<G>(total);
-    } else if (softmax && !a.renorm) {
-        // fp32 exponentials: |z - top| 2^-23 + 2^-23 of each, 2^-20 of the sum
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            total += z[r] > -INFINITY ? (double)__expf(z[r] - top) : 0.0;
         total = row_sum<G>(total);
     }
 
@@ -616,8 +613,10 @@ __global__ __launch_bounds__(kRouteWaves* kWave, kPlain ? 6 : 4) void route_forw
 //   given,   renormalised: dz_j = (g_j - sum g w) / S;  not: g_j
 // times scale; g_i = 0 where i was not chosen, and only the softmax that is
 // not renormalised has a gradient there.  A row without choice has none.
-// The row is put together in LDS and written once: 32,768 x 256 fp32 11 us,
-// 3.0 TB/s of writes.
+// The row is put together in LDS and written once: 32,768 x 256 fp32 10 us,
+// 3.3 TB/s of writes; the softmax that is not renormalised, which takes an
+// fp64 exponential of every score, 65,536 x 256 bf16 34 us (22 in fp32, whose
+// sum and p do not agree: 1 - sum p of the chosen is lost below 1e-8).
 template <class T, int G, int R>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(RouteArgs a, bool fours)
 {
@@ -644,27 +643,30 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
     const bool whole = a.score == SOFT_TOPK_SCORE_SOFTMAX && !a.renorm;
     double p = 0.0, dz = 0.0, spread = 0.0;
     if (whole) {
+        // fp64 all along: g - spread cancels where the chosen hold nearly all of the row, and the sum has to be
+        // that of the very p it is formed with
         float v[R], top = -INFINITY;
         load_row<T, G, R>(a.z, t * E, E, own, live, fours, v);
 #pragma unroll
         for (int r = 0; r < R; ++r)
             top = fmaxf(top, v[r]);
         top = row_max<G>(top);
-        double sum = 0.0;
+        double part[R], sum = 0.0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            v[r] = any && v[r] > -INFINITY ? __expf(v[r] - top) : 0.0f;
-            sum += (double)v[r];
+            part[r] = any && v[r] > -INFINITY ? exp64((double)v[r] - (double)top) : 0.0;
+            sum += part[r];
         }
         sum = row_sum<G>(sum);
         p = e >= 0 ? exp64(z - (double)top) / sum : 0.0;
         spread = row_sum<G>(g * p);
         dz = p * (g - spread);
-        const float f = any ? (float)(-spread / sum) : 0.0f;
+        const double f = any ? -spread / sum : 0.0;
 #pragma unroll
         for (int c = 0; c < R / 4; ++c)
             *reinterpret_cast<float4*>(out + (c * G + own) * 4) =
-                make_float4(v[c * 4] * f, v[c * 4 + 1] * f, v[c * 4 + 2] * f, v[c * 4 + 3] * f);
+                make_float4((float)(part[c * 4] * f), (float)(part[c * 4 + 1] * f), (float)(part[c * 4 + 2] * f),
+                            (float)(part[c * 4 + 3] * f));
     } else {
 #pragma unroll
         for (int c = 0; c < R / 4; ++c)

@@ -115,3 +115,50 @@ def test_residual_gradient_captured_and_replayed(dev):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(out.cpu(), residual_gradient(dy.cpu(), [kept]))
+
+
+# ---- softmax over the whole row ------------------------------------------------
+
+WHOLE = [(3, 2, 1, "f32"), (70, 60, 4, "f32"), (33, 256, 8, "bf16"), (9, 500, 16, "f16"), (5, 1024, 32, "f32")]
+
+
+@pytest.mark.parametrize("T,E,k,dtype", WHOLE)
+@pytest.mark.parametrize("grouped", [False, True])
+def test_softmax_weights_are_rounded_once(dev, T, E, k, dtype, grouped):
+    z = (torch.randn(T, E, generator=gen(E)) * 4).to(base.DTYPES[dtype])
+    options = dict(renormalize=False)
+    if grouped:
+        options.update(n_group=2, topk_group=2)
+    w, e = stk.route(z.to(dev), k, **options)
+    want_w, want_e = ref.route(z, k, **options)
+    assert torch.equal(e.cpu(), want_e)
+    within(w, want_w, want_w * 1.01 * ref.U32 + 1e-40, "weights")
+
+
+@pytest.mark.parametrize("E", [1, 4, 16, 31])
+def test_softmax_gradient_of_the_whole_sum_is_none(dev, E):
+    # all chosen and equal cotangents: sum p = 1, so the gradient is 0; what is left are some E + 8 fp64 roundings of p
+    z = torch.randn(40, E, generator=gen(E)) * 3
+    zd = z.to(dev).requires_grad_(True)
+    w, _ = stk.route(zd, E, renormalize=False)
+    (dz,) = torch.autograd.grad(w, [zd], torch.full((40, E), 0.75, device=dev))
+    p = torch.softmax(z.double(), 1)
+    within(dz, torch.zeros(40, E, dtype=torch.float64), p * 0.75 * (E + 8) * 2.0 ** -52 + 1e-40, "dz")
+
+
+@pytest.mark.parametrize("E,k,dtype", [(64, 4, "f32"), (256, 8, "f32"), (300, 12, "f16"), (1000, 20, "bf16")])
+def test_softmax_gradient_where_the_chosen_hold_nearly_all(dev, E, k, dtype):
+    # dz = p (g - sum g p) with equal g: p g (1 - sum of the chosen p), some 1e-7 of p g; a sum and a p that agree to
+    # 2^-52 leave (E + 8) 2^-52 p g beside the rounding of the result
+    z = torch.randn(20, E, generator=gen(k)) * 0.5 - 18
+    for t in range(20):
+        z[t, torch.randperm(E, generator=gen(t))[:k]] += 18
+    z = z.to(base.DTYPES[dtype])
+    zd = z.to(dev).requires_grad_(True)
+    w, e = stk.route(zd, k, renormalize=False)
+    g = torch.full((20, k), 1.25)
+    (dz,) = torch.autograd.grad(w, [zd], g.to(dev))
+    want = ref.route_grad(z, e.cpu(), g, renormalize=False)
+    p = torch.softmax(z.double(), 1)
+    within(dz, want, want.abs() * (1.01 * ref.half_step(z.dtype) + 2.0 ** -22) + p * 1.25 * (E + 8) * 2.0 ** -52
+           + ref.tiny(z.dtype), "dz")
