@@ -5,7 +5,7 @@
 // Row r of expert e (offsets[e] <= r < offsets[e + 1]), source s = rows[r]
 // (r itself without rows):
 //   z_r = W_e x_s + b_e;  y_r = act(z_r) + residual_r
-// act: none, silu z s(z), gelu z Phi(z) (exact, by erf), or swiglu, whose W_e
+// act: none, silu z s(z), gelu z Phi(z) (exact, by erfc), or swiglu, whose W_e
 // has 2 N rows: y = silu(z[:N]) z[N:].  Backward, with dz = dy act'(z):
 //   dx_s = sum over the places of s of W_e^T dz_r;  dW_e = sum_r dz_r x_s^T;
 //   db_e = sum_r dz_r
@@ -499,7 +499,9 @@ __device__ __forceinline__ void step_mma(const char* lds, int p0, int q0, V4F (&
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 __device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
-__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.0f + erff(z * 0.70710678f)); }
+// Phi(z) by erfc, which keeps the negative tail (1 + erf is off by 4% at -5 and 0 from -5.6 on)
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678f); }
+__device__ __forceinline__ float gelu(float z) { return z * normal_cdf(z); }
 
 __device__ __forceinline__ float act_slope(int act, float z)
 {
@@ -508,7 +510,7 @@ __device__ __forceinline__ float act_slope(int act, float z)
         return s * (1.0f + z * (1.0f - s));
     }
     if (act == SOFT_TOPK_ACT_GELU)
-        return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+        return normal_cdf(z) + z * 0.39894228f * __expf(-0.5f * z * z);
     return 1.0f;
 }
 

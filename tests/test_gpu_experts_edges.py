@@ -162,3 +162,32 @@ def test_softmax_gradient_where_the_chosen_hold_nearly_all(dev, E, k, dtype):
     p = torch.softmax(z.double(), 1)
     within(dz, want, want.abs() * (1.01 * ref.half_step(z.dtype) + 2.0 ** -22) + p * 1.25 * (E + 8) * 2.0 ** -52
            + ref.tiny(z.dtype), "dz")
+
+
+# ---- tails of the activations ---------------------------------------------------
+
+def tail(dtype):
+    z = -torch.arange(1, 401).double() / 32  # to -12.5, where z Phi(z) is 5e-35
+    return z.to(base.DTYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gelu_keeps_its_negative_tail(dev, dtype):
+    # x = z, w = 1: z itself.  Phi(z) = erfc(-z / sqrt 2) / 2, whose argument is off by 2 2^-24 of itself: (z^2 + 2)
+    # 2^-23 of the value; erfc by some 16 2^-24; the product and the rounding of y
+    x = tail(dtype)[:, None]
+    w = torch.ones(1, 1, 1, dtype=x.dtype)
+    offsets = torch.tensor([0, len(x)], dtype=torch.int32)
+    xd = x.to(dev).requires_grad_(True)
+    y = stk.experts_product(xd, w.to(dev), stk.Dispatch(offsets.to(dev)), act="gelu")
+    z = x.double()
+    cdf = torch.special.erfc(-z / math.sqrt(2.0)) / 2
+    value = z * cdf
+    rel = (32 + 2 * z * z) * ref.U32
+    within(y, value, value.abs() * (rel + 1.01 * ref.half_step(x.dtype)) + ref.tiny(x.dtype), "y")
+    # the slope Phi(z) + z phi(z): the exponential's argument is off by some 4 2^-24 of itself
+    (dx,) = torch.autograd.grad(y, [xd], torch.ones_like(y))
+    bell = z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    slope = cdf + bell
+    bound = (cdf + bell.abs()) * (32 + 4 * z * z) * ref.U32
+    within(dx, slope, bound + slope.abs() * 1.01 * ref.half_step(x.dtype) + ref.tiny(x.dtype), "dx")
