@@ -138,6 +138,8 @@ def load():
     lib.soft_topk_experts_residual_backward.restype = ctypes.c_int
     lib.soft_topk_combine_forward.argtypes = [vp, fp, vp, vp, i32, i64, i32, i64, i32, vp, vp]
     lib.soft_topk_combine_forward.restype = ctypes.c_int
+    lib.soft_topk_combine_forward_ex.argtypes = [vp, fp, vp, vp, i32, i64, i32, i64, i32, i32, vp, vp]
+    lib.soft_topk_combine_forward_ex.restype = ctypes.c_int
     lib.soft_topk_combine_backward.argtypes = [vp, vp, fp, vp, i32, i64, i32, i64, i32, vp, fp, vp, sz, vp]
     lib.soft_topk_combine_backward.restype = ctypes.c_int
     lib.soft_topk_strerror.argtypes = [ctypes.c_int]

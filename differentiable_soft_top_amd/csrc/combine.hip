@@ -6,6 +6,8 @@
 // once.  Backward: dy[slot_tj] = w_tj dout_t, dw_tj = <dout_t, y[slot_tj]>
 // (0 for a dropped choice), and the rows of dy behind the last place are 0.
 // Every place belongs to one pair, so dy is written without atomics.
+// A choice without a place is left out whatever its weight; with keep_nan a
+// NaN weight there counts (times a row of zeros) and the token is NaN.
 //
 // Bound by memory: every row of y is read once (and of dy written once).  A
 // token has a group of 8 to 256 lanes, by its length, each on eight
@@ -112,6 +114,9 @@ __global__ __launch_bounds__(kThreads) void combine_forward_kernel(CombineArgs a
                 if (place >= 0 && place < a.places) {
                     w[j] = a.w ? a.w[t * a.k + j0 + j] : 1.0f;
                     y[j].load(a.y, (int64_t)place * a.N + n, count, kWhole);
+                } else if (a.keep_nan && j0 + j < a.k) {
+                    const float lost = a.w[t * a.k + j0 + j];
+                    w[j] = lost != lost ? lost : 0.0f;  // times a row of zeros
                 }
             }
             if (j0 == 0)

@@ -252,12 +252,12 @@ int soft_topk_experts_residual_backward(const void* grad_y, int32_t dtype, const
     return done(launch_experts_residual(a, grad_residual, static_cast<hipStream_t>(stream)));
 }
 
-int soft_topk_combine_forward(const void* y, const float* weights, const int32_t* slots, const void* residual,
-                              int32_t dtype, int64_t tokens, int32_t k, int64_t places, int32_t N, void* out,
-                              void* stream)
+int soft_topk_combine_forward_ex(const void* y, const float* weights, const int32_t* slots, const void* residual,
+                                 int32_t dtype, int64_t tokens, int32_t k, int64_t places, int32_t N, int32_t flags,
+                                 void* out, void* stream)
 {
     if (!y || !weights || !slots || !out || !any_type(dtype) || !in_range(tokens) || k < 1 || tokens * k > kMax32 ||
-        !in_range(places) || N < 1)
+        !in_range(places) || N < 1 || (flags & ~SOFT_TOPK_COMBINE_KEEP_NAN))
         return SOFT_TOPK_EINVAL;
     CombineArgs a;
     memset(&a, 0, sizeof(a));
@@ -269,8 +269,16 @@ int soft_topk_combine_forward(const void* y, const float* weights, const int32_t
     a.k = k;
     a.places = (int32_t)places;
     a.N = N;
+    a.keep_nan = flags & SOFT_TOPK_COMBINE_KEEP_NAN;
     a.out = out;
     return done(launch_combine_forward(a, dtype, dtype == SOFT_TOPK_F32, static_cast<hipStream_t>(stream)));
+}
+
+int soft_topk_combine_forward(const void* y, const float* weights, const int32_t* slots, const void* residual,
+                              int32_t dtype, int64_t tokens, int32_t k, int64_t places, int32_t N, void* out,
+                              void* stream)
+{
+    return soft_topk_combine_forward_ex(y, weights, slots, residual, dtype, tokens, k, places, N, 0, out, stream);
 }
 
 int soft_topk_combine_backward(const void* grad_out, const void* y, const float* weights, const int32_t* slots,

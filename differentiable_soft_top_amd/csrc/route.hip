@@ -612,7 +612,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave, kPlain ? 6 : 4) void route_forw
 //   sigmoid, renormalised: dz_j = (1 - s_j) w_j (g_j - sum g w);  not: g_j s_j (1 - s_j)
 //   given,   renormalised: dz_j = (g_j - sum g w) / S;  not: g_j
 // times scale; g_i = 0 where i was not chosen, and only the softmax that is
-// not renormalised has a gradient there.  A row without choice has none.
+// not renormalised has a gradient there.  A row without choice has none: 0,
+// or NaN where its scores hold a NaN or +inf.
 // The row is put together in LDS and written once: 32,768 x 256 fp32 10 us,
 // 3.3 TB/s of writes; the softmax that is not renormalised, which takes an
 // fp64 exponential of every score, 65,536 x 256 bf16 34 us (22 in fp32, whose
@@ -640,6 +641,16 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
         }
     }
     const bool any = row_ballot<G>(e >= 0) != 0;
+    // a row without choice may be one that is not finite
+    bool bad = false;
+    if (__ballot(live && !any) != 0ull) {
+        float v[R];
+        load_row<T, G, R>(a.z, t * E, E, own, live && !any, fours, v);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            bad |= !(v[r] < INFINITY);
+        bad = row_ballot<G>(bad) != 0;
+    }
     const bool whole = a.score == SOFT_TOPK_SCORE_SOFTMAX && !a.renorm;
     double p = 0.0, dz = 0.0, spread = 0.0;
     if (whole) {
@@ -708,6 +719,11 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_backward_kernel(Rout
     lds_order();
     if (first)
         out[e] = (float)mine;
+    if (bad) {
+#pragma unroll
+        for (int c = 0; c < R / 4; ++c)
+            *reinterpret_cast<float4*>(out + (c * G + own) * 4) = make_float4(NAN, NAN, NAN, NAN);
+    }
     lds_order();
     if (!live)
         return;

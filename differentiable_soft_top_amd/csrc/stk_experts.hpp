@@ -104,6 +104,7 @@ struct CombineArgs {
     const int32_t* slots;     // [tokens][k]
     const void* residual;     // [tokens][N] or null
     int32_t tokens, k, places, N;
+    int32_t keep_nan;         // forward: a NaN weight without a place counts
     void* out;                // forward: [tokens][N]
     const void* dout;         // backward: [tokens][N]
     void* dy;                 // backward: [places][N] or null

@@ -316,16 +316,18 @@ def _combine_sizes(y, weights, slots, residual):
     return T, k, y.shape[0], y.shape[1]
 
 
-def combine_forward(y, weights, slots, residual=None):
-    """soft_topk_combine_forward: residual + the weighted sum of every token's rows of y, [tokens, N]."""
+def combine_forward(y, weights, slots, residual=None, keep_nan: bool = False):
+    """soft_topk_combine_forward_ex: residual + the weighted sum of every token's rows of y, [tokens, N]; with
+    ``keep_nan`` a NaN weight without a row (slot -1) makes the token's sum NaN."""
     torch, lib = _load()
     T, k, places, N = _combine_sizes(y, weights, slots, residual)
     dev = y.device
     with _on(dev):
         out = y.new_empty((T, N))
-        rc = lib.soft_topk_combine_forward(y.data_ptr(), weights.data_ptr(), slots.data_ptr(), _ptr(residual),
-                                           _TYPES[y.dtype], T, k, places, N, out.data_ptr(), _stream(dev))
-    _lib.check(rc, "soft_topk_combine_forward")
+        rc = lib.soft_topk_combine_forward_ex(y.data_ptr(), weights.data_ptr(), slots.data_ptr(), _ptr(residual),
+                                              _TYPES[y.dtype], T, k, places, N, 1 if keep_nan else 0, out.data_ptr(),
+                                              _stream(dev))
+    _lib.check(rc, "soft_topk_combine_forward_ex")
     return out
 
 
@@ -414,14 +416,14 @@ def _functions():
         if g is not None and (want[0] or want[1]):
             y, weights, slots = ctx.saved_tensors
             dy, dw = _combine_backward(g.contiguous(), y, weights, slots, want)
-        return dy, dw, None, g if want[3] else None
+        return dy, dw, None, g if want[3] else None, None
 
     class _Combine(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, y, weights, slots, residual):
+        def forward(ctx, y, weights, slots, residual, keep_nan):
             ctx.save_for_backward(y, weights, slots)
             ctx.set_materialize_grads(False)
-            return combine_forward(y, weights, slots, residual)
+            return combine_forward(y, weights, slots, residual, keep_nan)
 
         backward = once(combine_grad)
 
@@ -463,13 +465,14 @@ def experts_product(x, w, plan: Dispatch, bias=None, act: str = "none", residual
     return experts_forward(x, w, plan, bias, act, residual)
 
 
-def combine(y, weights, slots, residual=None):
+def combine(y, weights, slots, residual=None, keep_nan: bool = False):
     """Differentiable weighted sum: out[t] = residual[t] + sum_j weights[t, j] y[slots[t, j]] (fp32 sums, -1
-    left out).  The kept slots hold the places from 0 once each, as dispatch writes them."""
+    left out).  The kept slots hold the places from 0 once each, as dispatch writes them.  ``keep_nan``: a NaN
+    weight whose slot is -1, as route writes them for a row of scores that is not finite, makes out[t] NaN."""
     _load()
     if _wants_grad(y, weights, residual):
-        return _functions()[2].apply(y, weights, slots, residual)
-    return combine_forward(y, weights, slots, residual)
+        return _functions()[2].apply(y, weights, slots, residual, keep_nan)
+    return combine_forward(y, weights, slots, residual, keep_nan)
 
 
 def moe(x, scores, w_up, w_down, k: int, act: str = "swiglu", bias_up=None, bias_down=None, residual=None,
@@ -477,9 +480,11 @@ def moe(x, scores, w_up, w_down, k: int, act: str = "swiglu", bias_up=None, bias
     """A layer of experts: every token through its k chosen ones, weighted, plus ``residual``.
 
     x: [tokens, K]; scores: [tokens, experts]; w_up: [experts, M, K]; w_down: [experts, K, N].  ``routing``:
-    the options of route.  Returns (out [tokens, K], experts int32 [tokens, k])."""
+    the options of route.  Returns (out [tokens, K], experts int32 [tokens, k]).  A token whose row of scores
+    holds a NaN or +inf has experts -1, comes out NaN, and its row of the scores' gradient is NaN; a padding
+    token, whose scores are all -inf, has experts -1 and comes out as its residual (or 0)."""
     weights, experts = route(scores, k, **routing)
     plan = dispatch(experts, scores.shape[1])
     h = experts_product(x, w_up, plan, bias=bias_up, act=act)
     y = experts_product(h, w_down, Dispatch(plan.offsets), bias=bias_down)
-    return combine(y, weights, plan.slots, residual=residual), experts
+    return combine(y, weights, plan.slots, residual=residual, keep_nan=True), experts

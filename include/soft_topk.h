@@ -423,8 +423,8 @@ int soft_topk_route_forward(const void* scores, int32_t dtype, int64_t tokens, i
  * Gradient of the weights with respect to the scores.  grad_weights:
  * fp32[tokens][k]; chosen: the forward's out_experts; grad_scores:
  * [tokens][experts] of `dtype`, all written.  A chosen index outside
- * [0, experts) takes no part; a row without one gets 0.  Errors as the
- * forward.
+ * [0, experts) takes no part; a row without one gets 0, or NaN where its
+ * scores hold a NaN or +inf.  Errors as the forward.
  */
 int soft_topk_route_backward(const float* grad_weights, const void* scores, int32_t dtype, int64_t tokens,
                              int32_t experts, const soft_topk_route* route, const int32_t* chosen,
@@ -515,6 +515,19 @@ int soft_topk_experts_residual_backward(const void* grad_y, int32_t dtype, const
 int soft_topk_combine_forward(const void* y, const float* weights, const int32_t* slots, const void* residual,
                               int32_t dtype, int64_t tokens, int32_t k, int64_t places, int32_t N, void* out,
                               void* stream);
+
+/*
+ * soft_topk_combine_forward, with SOFT_TOPK_COMBINE_KEEP_NAN in flags: a
+ * choice without a place whose weight is NaN makes its token's row NaN
+ * (soft_topk_route_forward marks a row of scores that is not finite so, and
+ * a padding row, which has weights 0, not).  The gradients are those of
+ * soft_topk_combine_backward: such a choice counts NaN times no row.  flags:
+ * 0 or SOFT_TOPK_COMBINE_KEEP_NAN, else EINVAL.
+ */
+#define SOFT_TOPK_COMBINE_KEEP_NAN 1
+int soft_topk_combine_forward_ex(const void* y, const float* weights, const int32_t* slots, const void* residual,
+                                 int32_t dtype, int64_t tokens, int32_t k, int64_t places, int32_t N, int32_t flags,
+                                 void* out, void* stream);
 
 /*
  * Gradients of soft_topk_combine_forward (the residual's is grad_out).

@@ -23,6 +23,14 @@ def test_residual_refusals(lib):
         assert call(**bad) == _lib.EINVAL, bad
 
 
+def test_combine_refuses_unknown_flags(lib):
+    def call(y=FAKE, T=4, k=2, P=8, N=16, flags=0):
+        return lib.soft_topk_combine_forward_ex(y, FAKE, FAKE, None, 1, T, k, P, N, flags, FAKE, None)
+
+    for bad in (dict(flags=2), dict(flags=-1), dict(y=None), dict(T=0), dict(k=0), dict(P=0), dict(N=0)):
+        assert call(**bad) == _lib.EINVAL, bad
+
+
 def test_residual_refuses_host_tensors():
     import torch
 

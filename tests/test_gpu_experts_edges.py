@@ -191,3 +191,86 @@ def test_gelu_keeps_its_negative_tail(dev, dtype):
     slope = cdf + bell
     bound = (cdf + bell.abs()) * (32 + 4 * z * z) * ref.U32
     within(dx, slope, bound + slope.abs() * 1.01 * ref.half_step(x.dtype) + ref.tiny(x.dtype), "dx")
+
+
+# ---- router rows that are not finite ---------------------------------------------
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid", "given"])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_layer_shows_a_router_row_that_is_not_finite(dev, score, with_residual):
+    # tokens 3 and 70 have a broken row of scores, token 5 is padding
+    x, scores, w_up, w_down = base.layer_inputs()
+    padded = scores.clone()
+    padded[[3, 5, 70]] = -math.inf
+    scores[5] = -math.inf
+    scores[3, 7] = math.nan
+    scores[70, 0] = math.inf
+    leaves = [t.to(dev).requires_grad_(True) for t in (x, scores, w_up, w_down)]
+    residual = leaves[0] if with_residual else None
+    out, experts = stk.moe(*leaves, 3, residual=residual, score=score)
+    want, _ = stk.moe(x.to(dev), padded.to(dev), w_up.to(dev), w_down.to(dev), 3,
+                      residual=x.to(dev) if with_residual else None, score=score)
+    broken = torch.zeros(x.shape[0], dtype=torch.bool, device=dev)
+    broken[[3, 70]] = True
+    assert (experts[[3, 5, 70]] == -1).all()
+    assert torch.isnan(out[broken]).all()
+    assert torch.equal(out[~broken], want[~broken])
+    assert torch.equal(out[5], x[5].to(dev) if with_residual else torch.zeros_like(out[5]))
+    grads = torch.autograd.grad(out, leaves, torch.ones_like(out))
+    assert torch.isnan(grads[1][broken]).all()
+    assert torch.isfinite(grads[1][~broken]).all() and (grads[1][5] == 0).all()
+    for i in (0, 2, 3):  # no expert saw the broken tokens
+        assert torch.isfinite(grads[i]).all()
+
+
+@pytest.mark.parametrize("E,k", [(12, 3), (256, 8), (500, 16), (1000, 32)])
+@pytest.mark.parametrize("options", [dict(), dict(renormalize=False), dict(score="sigmoid"),
+                                     dict(score="sigmoid", renormalize=False), dict(score="given"),
+                                     dict(score="given", renormalize=False)])
+def test_route_gradient_of_rows_that_are_not_finite(dev, E, k, options):
+    z = torch.rand(70, E, generator=gen(E)) + 0.5
+    clean = z.to(dev).requires_grad_(True)
+    g = torch.randn(70, k, generator=gen(k)).to(dev)
+    (want,) = torch.autograd.grad(stk.route(clean, k, **options)[0], [clean], g)
+    z[1, E - 1] = math.nan
+    z[17, 0] = math.inf
+    z[69, E // 2] = math.inf
+    z[33] = -math.inf
+    leaf = z.to(dev).requires_grad_(True)
+    (dz,) = torch.autograd.grad(stk.route(leaf, k, **options)[0], [leaf], g)
+    assert torch.isnan(dz[[1, 17, 69]]).all()
+    assert (dz[33] == 0).all()
+    rest = torch.ones(70, dtype=torch.bool, device=dev)
+    rest[[1, 17, 33, 69]] = False
+    assert torch.equal(dz[rest], want[rest])
+
+
+@pytest.mark.parametrize("T,k,N,dtype", [(9, 2, 40, "bf16"), (20, 12, 37, "f16"), (3, 8, 2048, "f32")])
+def test_combine_keeps_the_nan_of_dropped_choices_when_asked(dev, T, k, N, dtype):
+    y, w, slots, res, dout = base.combine_inputs(T, k, N, dtype, True, 0.3)
+    slots[1] = slots[0, k - 1] = -1
+    kept = slots >= 0
+    slots[kept] = torch.randperm(int(kept.sum()), generator=gen(N)).to(torch.int32)
+    w[~kept] = 0.5  # finite: left out as ever
+    slots[0, k - 1] = T * k + 3  # no place either
+    clean = w.clone()
+    w[0, k - 1] = math.nan
+    w[1, 0] = math.nan
+    args = [t.to(dev) for t in (y, w, slots, res)]
+    out = stk.combine(*args, keep_nan=True)
+    value, bound = ref.combine(y, clean, slots, res)[0]
+    assert torch.isnan(out[:2]).all()
+    within(out[2:], value[2:], bound[2:], "out")
+    within(stk.combine(*args), value, bound, "out, NaN left out")
+    yd = args[0].requires_grad_(True)
+    a = torch.autograd.grad(stk.combine(yd, *args[1:], keep_nan=True), [yd], dout.to(dev))[0]
+    b = torch.autograd.grad(stk.combine(yd, *args[1:]), [yd], dout.to(dev))[0]
+    assert torch.equal(a, b)
+
+
+def test_layer_with_a_nan_bias_is_nan(dev):
+    x, scores, w_up, w_down = (t.to(dev) for t in base.layer_inputs())
+    bias = torch.zeros(12, device=dev)
+    bias[4] = math.nan
+    out, experts = stk.moe(x, scores, w_up, w_down, 3, residual=x, bias=bias)
+    assert torch.isnan(out).all() and (experts == -1).all()
