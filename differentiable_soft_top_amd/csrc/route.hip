@@ -36,6 +36,7 @@ namespace stk {
 namespace {
 
 constexpr int kRouteWaves = 4;  // of a work-group
+constexpr float kLowest = -3.402823466e38f;
 
 template <class T>
 __device__ __forceinline__ float load_up(const void* p, int64_t i)
@@ -459,7 +460,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave, kPlain ? 6 : 4) void route_forw
                 v[r] = __builtin_amdgcn_rcpf(1.0f + __expf(-z[r]));
             else if (softmax)
                 v[r] = __expf(z[r] - top) * unit;
-            v[r] = z[r] > -INFINITY ? v[r] + b[r] : -INFINITY;
+            // (a sum below the lowest number counts as it: u, in fp64, is one)
+            v[r] = fminf(z[r], b[r]) > -INFINITY ? fmaxf(v[r] + b[r], kLowest) : -INFINITY;
             high = fmaxf(high, v[r] > -INFINITY ? fabsf(v[r]) : 0.0f);
         }
         // sigmoid and exponential: below 2^-22 each (|z| e^-|z| < 0.4); the sum rounds by 2^-24 of itself
@@ -487,7 +489,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave, kPlain ? 6 : 4) void route_forw
                 group_best<1>(values, from, part, size, turn, best, second);
             // one lane speaks for its group
             const bool speaks = group < a.n_group && part == 0;
-            float score = a.group_top == 2 && second > -INFINITY ? best + second : best;
+            float score = a.group_top == 2 && second > -INFINITY ? fmaxf(best + second, kLowest) : best;
             score = speaks ? score : -INFINITY;
             int ahead = 0;  // groups before this one
             row_others<G>(score, [&](float o) { ahead += o > score; });
@@ -530,7 +532,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave, kPlain ? 6 : 4) void route_forw
     // (at least the lowest number: -inf is no candidate)
     int above = 0;
     row_others<G>(mine, [&](float o) { above += o > mine; });
-    const float bound = fmaxf(row_min<G>(above < a.k ? mine : INFINITY) - 2.0f * error, -3.402823466e38f);
+    const float bound = fmaxf(row_min<G>(above < a.k ? mine : INFINITY) - 2.0f * error, kLowest);
     int held = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r)

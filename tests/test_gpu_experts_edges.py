@@ -274,3 +274,55 @@ def test_layer_with_a_nan_bias_is_nan(dev):
     bias[4] = math.nan
     out, experts = stk.moe(x, scores, w_up, w_down, 3, residual=x, bias=bias)
     assert torch.isnan(out).all() and (experts == -1).all()
+
+
+# ---- scores and biases at the type's lowest value ---------------------------------
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+def check_choice(dev, z, k, options):
+    want_w, want_e = ref.route(z, k, **options)
+    w, e = stk.route(z.to(dev), k, **base.on(options, dev))
+    assert torch.equal(e.cpu(), want_e)
+    within(w, want_w, want_w.abs() * 1.01 * ref.U32 + 1e-40, "weights")
+
+
+@pytest.mark.parametrize("E,k", [(8, 6), (60, 8), (256, 8), (512, 16), (1024, 32)])
+def test_lowest_score_with_a_lowering_bias_stays_available(dev, E, k):
+    # u = z + bias = -4.4e38 is a number (fp32 has none there): chosen after all others, lowest index first
+    z = torch.rand(20, E, generator=gen(E))
+    z[:, k // 2:] = LOWEST
+    bias = torch.zeros(E)
+    bias[k // 2:] = -1e38
+    check_choice(dev, z, k, dict(score="given", renormalize=False, bias=bias))
+    bias[E - 1] = -0.9e38  # now the last is the best of those
+    check_choice(dev, z, k, dict(score="given", renormalize=False, bias=bias))
+
+
+@pytest.mark.parametrize("E,k,groups,open_", [(16, 10, 4, 3), (60, 8, 6, 5), (256, 8, 8, 6), (512, 16, 32, 31),
+                                              (1024, 32, 64, 60)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid", "given"])
+def test_group_of_lowest_biases_stays_available(dev, E, k, groups, open_, score):
+    # a group whose two best are both at the lowest value has a sum (-6.8e38) that orders it last, ties by index
+    z = torch.rand(20, E, generator=gen(E)) + 0.5
+    size = E // groups
+    bias = torch.zeros(E)
+    bias[:(groups - 1) * size] = LOWEST
+    options = dict(score=score, bias=bias, n_group=groups, topk_group=open_, group_top=2, renormalize=False)
+    if size < k:
+        check_choice(dev, z, k, options)
+    bias[size:2 * size:2] = 0.25  # one or more of a group's two best
+    check_choice(dev, z, min(k, 8), options)
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_groups_of_lowest_scores(dev, group_top):
+    z = torch.rand(30, 64, generator=gen(6))
+    z[:, 8:40] = LOWEST
+    z[3] = LOWEST
+    z[4, ::2] = LOWEST
+    z[5] = 3e38
+    for open_ in (1, 3, 4, 6, 8):
+        check_choice(dev, z, 8, dict(score="given", n_group=8, topk_group=open_, group_top=group_top,
+                                     renormalize=False))
