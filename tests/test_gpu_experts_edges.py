@@ -326,3 +326,29 @@ def test_groups_of_lowest_scores(dev, group_top):
     for open_ in (1, 3, 4, 6, 8):
         check_choice(dev, z, 8, dict(score="given", n_group=8, topk_group=open_, group_top=group_top,
                                      renormalize=False))
+
+
+# ---- many groups --------------------------------------------------------------------
+
+@pytest.mark.parametrize("E,k,groups,open_", [(256, 8, 32, 5), (255, 7, 17, 3), (256, 8, 64, 20), (128, 8, 64, 64),
+                                              (512, 16, 32, 9), (512, 12, 64, 11), (510, 16, 17, 4),
+                                              (1024, 32, 64, 12), (960, 20, 60, 9), (64, 1, 64, 1)])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_with_many_groups(dev, E, k, groups, open_, group_top, score):
+    print("[groups] E=%d k=%d %d of %d top %d %s" % (E, k, open_, groups, group_top, score), flush=True)
+    for masked, bias in ((0.0, True), (0.4, False)):
+        options = dict(score=score, bias=bias, n_group=groups, topk_group=open_, group_top=group_top, scale=1.5)
+        z, options = base.route_inputs(37, E, "f32", options, masked)
+        want_w, want_e = ref.route(z, k, **options)
+        zd = z.to(dev).requires_grad_(True)
+        w, e = stk.route(zd, k, **base.on(options, dev))
+        g = torch.randn(37, k, generator=gen(E))
+        (dz,) = torch.autograd.grad(w, [zd], g.to(dev))
+        assert torch.equal(e.cpu(), want_e)
+        within(w, want_w, want_w * 1.01 * ref.U32 + 1e-40, "weights")
+        want = ref.route_grad(z, want_e, g, **{n: v for n, v in options.items() if n != "bias"})
+        # renormalised: at the chosen only, in fp64; where its parts cancel (k = 1: to 0) some eight fp64 roundings of
+        # the parts remain on either side, 8 2^-53 scale |g| each
+        parts = 1.5 * g.abs().double().sum(1, keepdim=True) * 2.0 ** -49
+        within(dz, want, want.abs() * 1.01 * ref.U32 + parts + ref.tiny(torch.float32), "grad")
