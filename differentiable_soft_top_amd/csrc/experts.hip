@@ -47,7 +47,11 @@ __device__ __forceinline__ V4F mma(V8S p, V8S q, V4F c, F16)
 // ---- where a row tile lies -------------------------------------------------
 
 // The experts' row tiles, counted by every wave for itself: lane l sums the
-// tiles of its run of experts, a wave scan makes them places.
+// tiles of its run of experts, a wave scan makes them places.  Offsets that
+// fall may name more tiles than a launch has row tiles: a lane's are cut at
+// kMostTiles (a launch has fewer), so that the sums stay in 32 bits, and the
+// kernels take no more than they have.
+constexpr int kMostTiles = 1 << 24;
 struct Tiles {
     int per, mine, upto, total;  // experts per lane; this lane's tiles; up to and with it; all
     int start, end;              // rows of this lane's first expert
@@ -80,6 +84,7 @@ __device__ __forceinline__ Tiles count_tiles(const ExpertsArgs& a, int rows)
     for (int i = 1; i < t.per; ++i)
         if (first + i < a.experts)
             t.mine += expert_tiles(a, first + i, rows);
+    t.mine = t.mine < kMostTiles ? t.mine : kMostTiles;
     t.upto = t.mine;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
@@ -89,6 +94,14 @@ __device__ __forceinline__ Tiles count_tiles(const ExpertsArgs& a, int rows)
     }
     t.total = __builtin_amdgcn_readlane(t.upto, kWave - 1);
     return t;
+}
+
+// The row tiles that this launch of `across` columns works on: all of them,
+// unless the offsets fall.
+__device__ __forceinline__ int launched_tiles(const Tiles& t, int across)
+{
+    const int most = (int)gridDim.x / across;
+    return t.total < most ? t.total : most;
 }
 
 // The expert that holds row tile `tile` (below t.total), the first of its row
@@ -701,7 +714,7 @@ __global__ __launch_bounds__(S::kAll) void experts_forward_kernel(ExpertsArgs a)
     constexpr int kCols = kGated ? S::kBP / 2 : S::kBP;  // columns of y in a tile
     const Tiles t = count_tiles(a, S::kBQ);
     const int across = (a.N + kCols - 1) / kCols;
-    const int id = blockIdx.x, total = t.total * across;
+    const int id = blockIdx.x, total = launched_tiles(t, across) * across;
     if (id >= total) {
         const int over = id - total;
         const int64_t r0 = t.behind + (int64_t)(over / across) * S::kBQ;
@@ -909,7 +922,7 @@ __global__ __launch_bounds__(256) void experts_slope_kernel(ExpertsArgs a)
 constexpr int kBiasWaves = 16;
 
 template <class T>
-__global__ __launch_bounds__(kBiasWaves* kWave) void experts_bias_kernel(ExpertsArgs a)
+__global__ __launch_bounds__(kBiasWaves* kWave) void experts_bias_kernel(ExpertsArgs a, int tiles)
 {
     __shared__ float part[kBiasWaves][kWave];
     const Tiles t = count_tiles(a, kActRows);
@@ -917,7 +930,9 @@ __global__ __launch_bounds__(kBiasWaves* kWave) void experts_bias_kernel(Experts
     int first = __builtin_amdgcn_readlane(t.upto - t.mine, lane);
     for (int i = lane * t.per; i < e; ++i)
         first += expert_tiles(a, i, kActRows);
-    const int count = expert_tiles(a, e, kActRows);
+    // (within the table of tiles, where the offsets fall)
+    const int left = tiles - first, own = expert_tiles(a, e, kActRows);
+    const int count = own < left ? own : left;
     const int n = blockIdx.y * kWave + lane_id(), wave = threadIdx.x / kWave;
     float s = 0.0f;
     if (n < a.M) {
@@ -988,7 +1003,7 @@ __global__ __launch_bounds__(S::kAll) void experts_input_kernel(ExpertsArgs a)
     __shared__ __attribute__((aligned(16))) char lds_all[kTeam * S::kTeams];
     const Tiles t = count_tiles(a, S::kBQ);
     const int across = (a.K + S::kBP - 1) / S::kBP;
-    const int id = blockIdx.x, total = t.total * across;
+    const int id = blockIdx.x, total = launched_tiles(t, across) * across;
     if (id >= total) {
         const int over = id - total;
         const int64_t r0 = t.behind + (int64_t)(over / across) * S::kBQ;
@@ -1353,7 +1368,8 @@ hipError_t backward(const ExpertsArgs& a, int dtype, hipStream_t stream)
     }
     if (a.db) {
         const dim3 grid(a.experts, ceil_div(a.M, kWave));
-        STK_LAUNCH(kKExpertsBackward, stream, (experts_bias_kernel<T>), grid, dim3(kBiasWaves * kWave), 0, stream, a);
+        STK_LAUNCH(kKExpertsBackward, stream, (experts_bias_kernel<T>), grid, dim3(kBiasWaves * kWave), 0, stream, a,
+                   (int)experts_bias_tiles(a.pairs, a.experts));
     }
     if (a.dw) {
         const bool direct = chunks(a.x, a.K) && chunks(a.dz, a.M) && near(a);

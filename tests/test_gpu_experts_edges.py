@@ -352,3 +352,52 @@ def test_route_with_many_groups(dev, E, k, groups, open_, group_top, score):
         # the parts remain on either side, 8 2^-53 scale |g| each
         parts = 1.5 * g.abs().double().sum(1, keepdim=True) * 2.0 ** -49
         within(dz, want, want.abs() * 1.01 * ref.U32 + parts + ref.tiny(torch.float32), "grad")
+
+
+# ---- offsets that are not a dispatch's -------------------------------------------
+
+def fenced(shape, dtype, dev, fill):
+    """A tensor between two fences of 64 KiB each, and the whole storage."""
+    n = math.prod(shape)
+    pad = (1 << 16) // torch.empty(0, dtype=dtype).element_size()
+    store = torch.full((n + 2 * pad,), fill, dtype=dtype, device=dev)
+    return store[pad:pad + n].view(shape), store, pad
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("E,T,K,N", [(64, 700, 64, 96), (1024, 900, 72, 40), (3, 70, 33, 17), (512, 4096, 264, 264)])
+def test_product_with_wrong_offsets_stays_inside(dev, act, E, T, K, N):
+    # offsets that fall, leave [0, pairs] or name every row for every second expert: the results mean nothing, and
+    # nothing outside them is read (the library checks its own table) or written
+    lib = stk._lib.load()
+    bf = torch.bfloat16
+    code = {"none": 0, "gelu": 2, "swiglu": 3}[act]
+    M = 2 * N if act == "swiglu" else N
+    x, w = torch.ones(T, K, dtype=bf, device=dev), torch.ones(E, M, K, dtype=bf, device=dev)
+    b, dy = torch.ones(E, M, dtype=bf, device=dev), torch.ones(T, N, dtype=bf, device=dev)
+    wrong = [[T * (e % 2) for e in range(E + 1)], [T - e for e in range(E + 1)], [-5] * E + [2 ** 31 - 1],
+             [(-1) ** e * (2 ** 31 - 1) for e in range(E + 1)], [0] + [T] + [0] * (E - 1), [T] * (E + 1)]
+    for case in wrong:
+        offsets = torch.tensor(case, dtype=torch.int32, device=dev)
+        outs = {n: fenced(s, t, dev, 7.0) for n, (s, t) in dict(
+            y=((T, N), bf), z=((T, M), torch.float32), dx=((T, K), bf), dw=((E, M, K), bf), db=((E, M), bf),
+            dr=((T, N), bf)).items()}
+        p = {n: v[0].data_ptr() for n, v in outs.items()}
+        rc = lib.soft_topk_experts_forward(x.data_ptr(), w.data_ptr(), b.data_ptr(), None, 1, offsets.data_ptr(), None,
+                                           T, T, E, K, N, code, p["y"], p["z"], None)
+        assert rc == 0
+        torch.cuda.synchronize()
+        need = lib.soft_topk_experts_backward_workspace_bytes(T, E, K, N, code, 0)
+        ws, store, pad = fenced((need,), torch.uint8, dev, 7)
+        ws_ptr = (ws.data_ptr() + 255) // 256 * 256  # (the fence behind is 255 bytes nearer at most)
+        rc = lib.soft_topk_experts_backward(dy.data_ptr(), x.data_ptr(), w.data_ptr(), p["z"], 1, offsets.data_ptr(),
+                                            None, None, T, T, 1, E, K, N, code, p["dx"], p["dw"], p["db"], ws_ptr,
+                                            need, None)
+        assert rc == 0
+        torch.cuda.synchronize()
+        rc = lib.soft_topk_experts_residual_backward(dy.data_ptr(), 1, offsets.data_ptr(), T, E, N, p["dr"], None)
+        assert rc == 0
+        torch.cuda.synchronize()
+        for n, (t, whole, edge) in outs.items():
+            assert (whole[:edge] == 7).all() and (whole[whole.numel() - edge:] == 7).all(), (n, case[:4])
+        assert (store[:pad] == 7).all() and (store[store.numel() - pad + 256:] == 7).all()
