@@ -265,32 +265,62 @@ int token_lanes(int N)
     return lanes;
 }
 
-template <class T, class Y>
-hipError_t forward(const CombineArgs& a, hipStream_t stream)
+// Tokens t .. t + tokens - 1 of a call.
+template <class T>
+CombineArgs part_of(const CombineArgs& a, int64_t t, int32_t tokens)
 {
-    const int lanes = token_lanes(a.N), per = kThreads / lanes;
-    const dim3 grid((a.tokens + per - 1) / per), block(kThreads);
-    if (a.N % 8 == 0 && pieces(a.y) && pieces(a.residual) && pieces(a.out))
-        STK_LAUNCH(kKCombineForward, stream, (combine_forward_kernel<T, Y, true>), grid, block, 0, stream, a, lanes);
-    else
-        STK_LAUNCH(kKCombineForward, stream, (combine_forward_kernel<T, Y, false>), grid, block, 0, stream, a, lanes);
+    const int64_t row = (int64_t)a.N * sizeof(typename T::Store);
+    CombineArgs p = a;
+    p.tokens = tokens;
+    p.slots = a.slots + t * a.k;
+    p.w = a.w ? a.w + t * a.k : nullptr;
+    p.residual = a.residual ? static_cast<const char*>(a.residual) + t * row : nullptr;
+    p.out = a.out ? static_cast<char*>(a.out) + t * row : nullptr;
+    p.dout = a.dout ? static_cast<const char*>(a.dout) + t * row : nullptr;
+    p.dw = a.dw ? a.dw + t * a.k : nullptr;
+    return p;
+}
+
+template <class T, class Y>
+hipError_t forward(const CombineArgs& all, hipStream_t stream)
+{
+    const int lanes = token_lanes(all.N), per = kThreads / lanes;
+    const bool whole = all.N % 8 == 0 && pieces(all.y) && pieces(all.residual) && pieces(all.out);
+    for (int64_t t = 0; t < all.tokens; t += kLaunchTokens) {
+        const CombineArgs a = part_of<T>(all, t, (int32_t)(all.tokens - t < kLaunchTokens ? all.tokens - t : kLaunchTokens));
+        const dim3 grid((a.tokens + per - 1) / per), block(kThreads);
+        if (whole)
+            STK_LAUNCH(kKCombineForward, stream, (combine_forward_kernel<T, Y, true>), grid, block, 0, stream, a, lanes);
+        else
+            STK_LAUNCH(kKCombineForward, stream, (combine_forward_kernel<T, Y, false>), grid, block, 0, stream, a, lanes);
+    }
     return hipGetLastError();
 }
 
 template <class T>
-hipError_t backward(const CombineArgs& a, hipStream_t stream)
+hipError_t backward(const CombineArgs& all, hipStream_t stream)
 {
-    const int lanes = token_lanes(a.N), per = kThreads / lanes;
-    const int groups = (a.tokens + per - 1) / per;
-    const dim3 grid(groups + (a.dy ? kCounters : 0)), block(kThreads);
-    if (a.N % 8 == 0 && pieces(a.y) && pieces(a.dout) && pieces(a.dy))
-        STK_LAUNCH(kKCombineBackward, stream, (combine_backward_kernel<T, true>), grid, block, 0, stream, a, lanes,
-                   groups);
-    else
-        STK_LAUNCH(kKCombineBackward, stream, (combine_backward_kernel<T, false>), grid, block, 0, stream, a, lanes,
-                   groups);
-    if (a.dy)
-        STK_LAUNCH(kKCombineBackward, stream, (combine_rest_kernel<T>), dim3(256), block, 0, stream, a);
+    const int lanes = token_lanes(all.N), per = kThreads / lanes;
+    const bool whole = all.N % 8 == 0 && pieces(all.y) && pieces(all.dout) && pieces(all.dy);
+    // the choices are counted beside the tokens, or, where those take several launches, in one more
+    const bool one = all.tokens <= kLaunchTokens;
+    auto launch = [&](const CombineArgs& a, int groups, int counters) {
+        const dim3 grid(groups + counters), block(kThreads);
+        if (whole)
+            STK_LAUNCH(kKCombineBackward, stream, (combine_backward_kernel<T, true>), grid, block, 0, stream, a, lanes,
+                       groups);
+        else
+            STK_LAUNCH(kKCombineBackward, stream, (combine_backward_kernel<T, false>), grid, block, 0, stream, a, lanes,
+                       groups);
+    };
+    for (int64_t t = 0; t < all.tokens; t += kLaunchTokens) {
+        const CombineArgs a = part_of<T>(all, t, (int32_t)(all.tokens - t < kLaunchTokens ? all.tokens - t : kLaunchTokens));
+        launch(a, (a.tokens + per - 1) / per, all.dy && one ? kCounters : 0);
+    }
+    if (all.dy && !one)
+        launch(all, 0, kCounters);
+    if (all.dy)
+        STK_LAUNCH(kKCombineBackward, stream, (combine_rest_kernel<T>), dim3(256), dim3(kThreads), 0, stream, all);
     return hipGetLastError();
 }
 

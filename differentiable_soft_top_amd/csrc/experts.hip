@@ -1105,10 +1105,10 @@ __global__ __launch_bounds__(S::kAll) void experts_weight_kernel(ExpertsArgs a)
     const int c0 = j * S::kBP, m0 = i * S::kBQ;
     int row0 = clamp_row(a.offsets[e], a.pairs), end = clamp_row(a.offsets[e + 1], a.pairs);
     if (gridDim.y > 1) {  // this work-group's share of the expert's rows
-        const int share = (end - row0 + kBK * (int)gridDim.y - 1) / (kBK * (int)gridDim.y) * kBK;
-        const int64_t first = row0 + (int64_t)share * blockIdx.y;
+        const int64_t share = ((int64_t)end - row0 + kBK * gridDim.y - 1) / (kBK * (int64_t)gridDim.y) * kBK;
+        const int64_t first = row0 + share * blockIdx.y;
         row0 = first < end ? (int)first : end;
-        end = end - row0 < share ? end : row0 + share;
+        end = end - row0 < share ? end : row0 + (int)share;
     }
     int p0, q0;
     wave_place<S>(p0, q0);
@@ -1289,10 +1289,14 @@ bool near(const ExpertsArgs& a)
            (!a.rows || in_reach(a.tokens, a.K));
 }
 
+bool forward_direct(const ExpertsArgs& a) { return chunks(a.x, a.K) && chunks(a.w, a.K) && near(a); }
+bool weight_direct(const ExpertsArgs& a) { return chunks(a.x, a.K) && chunks(a.dz, a.M) && near(a); }
+bool input_direct(const ExpertsArgs& a) { return chunks(a.w, a.K) && chunks(a.dz, a.M) && near(a); }
+
 template <class T>
 hipError_t forward(const ExpertsArgs& a, hipStream_t stream)
 {
-    const bool direct = chunks(a.x, a.K) && chunks(a.w, a.K) && near(a);
+    const bool direct = forward_direct(a);
     const Size size = product_size(a, a.M, direct);
     if (size == Size::kTiny)
         direct ? forward_launch<T, Tiny, true>(a, stream) : forward_launch<T, Tiny, false>(a, stream);
@@ -1372,7 +1376,7 @@ hipError_t backward(const ExpertsArgs& a, int dtype, hipStream_t stream)
                    (int)experts_bias_tiles(a.pairs, a.experts));
     }
     if (a.dw) {
-        const bool direct = chunks(a.x, a.K) && chunks(a.dz, a.M) && near(a);
+        const bool direct = weight_direct(a);
         const int shares = experts_weight_shares(a.pairs, a.experts, a.K, a.M);
         const Size size = weight_size(a, direct);
         if (size == Size::kTiny)
@@ -1387,7 +1391,7 @@ hipError_t backward(const ExpertsArgs& a, int dtype, hipStream_t stream)
             weight_launch<T, Small, false>(a, 1, stream);
     }
     if (a.dx) {
-        const bool direct = chunks(a.w, a.K) && chunks(a.dz, a.M) && near(a);
+        const bool direct = input_direct(a);
         const Size size = product_size(a, a.K, direct);
         if (size == Size::kTiny)
             direct ? input_launch<T, Tiny, true>(a, stream) : input_launch<T, Tiny, false>(a, stream);
@@ -1416,7 +1420,46 @@ hipError_t backward(const ExpertsArgs& a, int dtype, hipStream_t stream)
     return hipGetLastError();
 }
 
+// f of the shape of that size
+template <class F>
+bool with_shape(Size size, const F& f)
+{
+    switch (size) {
+    case Size::kTiny: return f(Tiny{});
+    case Size::kMid: return f(Mid{});
+    case Size::kSmall: return f(Small{});
+    case Size::kWide: return f(Wide{});
+    default: return f(Big{});
+    }
+}
+
+bool launch_fits(int64_t groups, int threads) { return groups * threads < (1ll << 32); }
+
+// the row tiles of a product across `width` columns, `halves`: two of w to one
+bool product_fits(const ExpertsArgs& a, Size size, int width, int halves)
+{
+    return with_shape(size, [&](auto s) {
+        return launch_fits((int64_t)row_tiles(a, s.kBQ) * ceil_div(width, s.kBP / halves), s.kAll);
+    });
+}
+
 }  // namespace
+
+bool experts_forward_fits(const ExpertsArgs& a)
+{
+    return product_fits(a, product_size(a, a.M, forward_direct(a)), a.N, a.M != a.N ? 2 : 1);
+}
+
+bool experts_backward_fits(const ExpertsArgs& a)
+{
+    if ((a.dz != a.dy || a.db) && !launch_fits(row_tiles(a, kActRows), 256))
+        return false;
+    if (a.dw && !with_shape(weight_size(a, weight_direct(a)), [&](auto s) {
+            return launch_fits(weight_tiles(a.experts, a.K, a.M, s.kBP, s.kBQ), s.kAll);
+        }))
+        return false;
+    return !a.dx || product_fits(a, product_size(a, a.K, input_direct(a)), a.K, 1);
+}
 
 // Work-groups on the rows of one tile of dW: as many as fill the chip once,
 // each with four steps a team at least (65,536 rows of one expert, 256 x 256:

@@ -66,7 +66,7 @@ bool dispatch_ok(int64_t tokens, int32_t k, int32_t experts)
 }
 
 // The products' sizes, and that no grid of theirs leaves 31 bits (64 is the
-// smallest tile of the kernels that take many rows).
+// smallest tile; whether the launches fit is asked once they are chosen).
 bool product_ok(int32_t dtype, int64_t tokens, int64_t pairs, int32_t experts, int32_t K, int32_t N, int32_t act)
 {
     if (!half_type(dtype) || !in_range(tokens) || !in_range(pairs) || !experts_ok(experts) || K < 1 || N < 1)
@@ -191,6 +191,8 @@ int soft_topk_experts_forward(const void* x, const void* w, const void* bias, co
     a.rows = rows;
     a.y = out_y;
     a.z = out_z;
+    if (!experts_forward_fits(a))
+        return SOFT_TOPK_EINVAL;
     return done(launch_experts_forward(a, dtype, static_cast<hipStream_t>(stream)));
 }
 
@@ -233,6 +235,8 @@ int soft_topk_experts_backward(const void* grad_y, const void* x, const void* w,
     a.dxr = rows ? reinterpret_cast<float*>(base + p.dxr) : nullptr;
     a.dbp = reinterpret_cast<float*>(base + p.dbp);
     a.dwp = reinterpret_cast<float*>(base + p.dwp);
+    if (!experts_backward_fits(a))
+        return SOFT_TOPK_EINVAL;
     return done(launch_experts_backward(a, dtype, static_cast<hipStream_t>(stream)));
 }
 

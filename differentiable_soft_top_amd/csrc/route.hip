@@ -789,13 +789,30 @@ void route_typed(const RouteArgs& a, bool forward, hipStream_t stream)
 
 hipError_t route_by_type(const RouteArgs& a, int dtype, bool forward, hipStream_t stream)
 {
-    if (dtype == SOFT_TOPK_F32)
-        route_typed<F32>(a, forward, stream);
-    else if (dtype == SOFT_TOPK_BF16)
-        route_typed<Bf16>(a, forward, stream);
-    else
-        route_typed<F16>(a, forward, stream);
-    return hipGetLastError();
+    const int64_t row = (int64_t)a.experts * (dtype == SOFT_TOPK_F32 ? 4 : 2);  // bytes
+    for (int64_t t = 0; t < a.tokens; t += kLaunchTokens) {
+        RouteArgs part = a;
+        part.tokens = a.tokens - t < kLaunchTokens ? a.tokens - t : kLaunchTokens;
+        part.z = static_cast<const char*>(a.z) + t * row;
+        if (forward) {
+            part.weights = a.weights + t * a.k;
+            part.chosen = a.chosen + t * a.k;
+        } else {
+            part.chosen_in = a.chosen_in + t * a.k;
+            part.grad_w = a.grad_w + t * a.k;
+            part.grad_z = static_cast<char*>(a.grad_z) + t * row;
+        }
+        if (dtype == SOFT_TOPK_F32)
+            route_typed<F32>(part, forward, stream);
+        else if (dtype == SOFT_TOPK_BF16)
+            route_typed<Bf16>(part, forward, stream);
+        else
+            route_typed<F16>(part, forward, stream);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

@@ -40,6 +40,11 @@ struct F16 {
 // the hardware runs them in that order.
 __device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
 
+// A launch holds fewer than 2^32 work-items (of more it runs the remainder,
+// without an error); calls on more tokens than this go out in several (at
+// most 64 lanes a token in route.hip, 256 in combine.hip).
+constexpr int64_t kLaunchTokens = 1 << 23;
+
 // Row choice (route.hip): the limits the register layouts cover.
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxK = 32;
@@ -92,6 +97,9 @@ struct ExpertsArgs {
     float* dbp;               // backward workspace: column sums by row tiles
     float* dwp;               // backward workspace: dw by shares of the rows, where there are several
 };
+// whether every launch of the call holds fewer than 2^32 work-items
+bool experts_forward_fits(const ExpertsArgs& a);
+bool experts_backward_fits(const ExpertsArgs& a);
 hipError_t launch_experts_forward(const ExpertsArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_experts_backward(const ExpertsArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_experts_residual(const ExpertsArgs& a, void* dr, hipStream_t stream);  // dr: like y

@@ -467,7 +467,8 @@ size_t soft_topk_dispatch_workspace_bytes(int64_t tokens, int32_t k, int32_t exp
  * nothing outside); a row index outside [0, tokens) reads as a row of zeros.
  * 1 <= tokens, pairs, K, N < 2^31 - 512, M <= 4,194,176, experts <= 1024.
  * No workspace; asynchronous on `stream`.  Errors: EINVAL before any launch
- * (also where a launch would need 2^31 work-groups); EHIP.
+ * (also where a launch would need 2^32 work-items, from some 2^30 rows on);
+ * EHIP.
  */
 int soft_topk_experts_forward(const void* x, const void* w, const void* bias, const void* residual, int32_t dtype,
                               const int32_t* offsets, const int32_t* rows, int64_t tokens, int64_t pairs,

@@ -31,6 +31,23 @@ def test_combine_refuses_unknown_flags(lib):
         assert call(**bad) == _lib.EINVAL, bad
 
 
+def test_products_refuse_what_no_launch_holds(lib):
+    # 2^32 work-items: 256 to a tile of 128 rows, or of 64 rows of the activation's gradient
+    def fwd(R, K=1, N=1, act=0):
+        return lib.soft_topk_experts_forward(FAKE, FAKE, None, None, 1, FAKE, None, R, R, 1, K, N, act, FAKE, None, None)
+
+    def bwd(R, K=1, N=1, act=0, dx=FAKE, dw=FAKE, db=None):
+        return lib.soft_topk_experts_backward(FAKE, FAKE, FAKE, FAKE, 1, FAKE, None, None, R, R, 1, 1, K, N, act, dx, dw,
+                                              db, ctypes.c_void_p(0x200000), 1 << 50, None)
+
+    most = (1 << 31) - 600
+    assert fwd(most, N=130) == _lib.EINVAL  # ((2^31 - 600) / 128 + 1) 256 is still below, for one column of tiles
+    assert fwd(1 << 30, N=130) == _lib.EINVAL
+    assert bwd(most, K=130) == _lib.EINVAL
+    assert bwd((1 << 30) + 64, act=1, dx=None) == _lib.EINVAL
+    assert bwd((1 << 30) + 64, db=FAKE, dx=None) == _lib.EINVAL
+
+
 def test_residual_refuses_host_tensors():
     import torch
 

@@ -401,3 +401,80 @@ def test_product_with_wrong_offsets_stays_inside(dev, act, E, T, K, N):
         for n, (t, whole, edge) in outs.items():
             assert (whole[:edge] == 7).all() and (whole[whole.numel() - edge:] == 7).all(), (n, case[:4])
         assert (store[:pad] == 7).all() and (store[store.numel() - pad + 256:] == 7).all()
+
+
+# ---- more tokens than a launch holds -----------------------------------------------
+
+def test_route_of_more_tokens_than_a_launch_holds(dev):
+    # 2^28 rows at 16 lanes a row, 2^26 at 64: 2^32 work-items
+    for T, E, k in (((1 << 28) + 5, 1, 1), ((1 << 26) + 9, 18, 17)):
+        print("[route] T=%d E=%d k=%d" % (T, E, k), flush=True)
+        z = torch.rand(T, E, device=dev, dtype=torch.bfloat16)
+        w, e = stk.route_forward(z, k, score="given", renormalize=False)
+        at = torch.cat([torch.arange(c - 3, c + 3) for c in (3, 1 << 23, 1 << 24, 1 << 25, 1 << 26)]
+                       + [torch.arange(T - 5, T)])
+        at = at[at < T]
+        want_w, want_e = ref.route(z[at.to(dev)].cpu(), k, score="given", renormalize=False)
+        assert torch.equal(e[at.to(dev)].cpu(), want_e) and torch.equal(w[at.to(dev)].cpu().double(), want_w)
+        for first in range(0, T, 1 << 24):  # no row is left out
+            assert (e[first:first + (1 << 24)] >= 0).all()
+        g = w  # a cotangent at hand
+        dz = stk.route_backward(g, z, e, score="given", renormalize=False)
+        want = ref.route_grad(z[at.to(dev)].cpu(), want_e, g[at.to(dev)].cpu(), score="given", renormalize=False)
+        assert torch.equal(dz[at.to(dev)].cpu().double(), want)
+        if E == 1:
+            assert torch.equal(dz, z)
+        del z, w, e, g, dz
+        torch.cuda.empty_cache()
+
+
+def test_combine_of_more_tokens_than_a_launch_holds(dev):
+    # 256 lanes a token: 2^24 tokens are 2^32 work-items
+    T, N, P = (1 << 24) + 7, 1032, 500
+    slots = torch.full((T, 1), -1, dtype=torch.int32)
+    at = torch.cat([torch.arange(c, c + 60) for c in (0, (1 << 23) - 30, (1 << 24) - 55)])
+    at = torch.cat([at, torch.arange(T - 2, T)])
+    slots[at, 0] = torch.randperm(len(at), generator=gen(60)).to(torch.int32)
+    y = torch.randn(P, N, generator=gen(61)).to(torch.bfloat16)
+    w = torch.rand(T, 1, generator=gen(62))
+    yd, wd, sd = y.to(dev), w.to(dev), slots.to(dev)
+    out = stk.combine_forward(yd, wd, sd)
+    value, bound = ref.combine(y, w[at], slots[at], None)[0]
+    within(out[at.to(dev)], value, bound, "out")
+    assert (out[100:1000] == 0).all() and (out[(1 << 23) + 100:(1 << 23) + 1000] == 0).all()
+    dout = out.fill_(0)
+    some = torch.randn(len(at), N, generator=gen(63)).to(torch.bfloat16)
+    dout[at.to(dev)] = some.to(dev)
+    dy, dw = stk.combine_backward(dout, yd, wd, sd)
+    _, want_dy, want_dw = ref.combine(y, w[at], slots[at], None, some)
+    within(dy, *want_dy, "dy")
+    assert (dy[len(at):] == 0).all()
+    within(dw[at.to(dev)], *want_dw, "dw")
+    assert (dw[100:1000] == 0).all()
+    del out, dout
+    torch.cuda.empty_cache()
+
+
+def test_product_of_more_rows_than_31_bits_of_elements(dev):
+    R, K, N = (1 << 29) + 77, 8, 8  # 8.6e9 bytes of x, 4.3e9 elements
+    x = torch.zeros(R, K, dtype=torch.bfloat16, device=dev)
+    at = torch.cat([torch.arange(c, c + 9) for c in (0, 1 << 28, (1 << 29) - 4, R - 9)])
+    small = torch.randn(len(at), K, generator=gen(64)).to(torch.bfloat16)
+    x[at.to(dev)] = small.to(dev)
+    w = torch.randn(1, N, K, generator=gen(65)).to(torch.bfloat16)
+    off = torch.tensor([0, R], dtype=torch.int32)
+    y = stk.experts_product(x, w.to(dev), stk.Dispatch(off.to(dev)), act="silu")
+    few = torch.tensor([0, len(at)], dtype=torch.int32)
+    within(y[at.to(dev)], *ref.product(small, w, few, None, None, "silu", None)[0], "y")
+    assert (y[1000:100000] == 0).all()
+    del y
+    dy = torch.zeros(R, N, dtype=torch.bfloat16, device=dev)
+    dsmall = torch.randn(len(at), N, generator=gen(66)).to(torch.bfloat16)
+    dy[at.to(dev)] = dsmall.to(dev)
+    dx, dw, db = stk.experts_backward(dy, x, w.to(dev), stk.Dispatch(off.to(dev)), want=(True, True, True))
+    _, want_dx, want_dw, want_db = ref.product(small, w, few, None, None, "none", None, dsmall)
+    within(dx[at.to(dev)], *want_dx, "dx")
+    within(dw, *want_dw, "dw")
+    within(db, *want_db, "db")
+    del x, dy, dx
+    torch.cuda.empty_cache()
