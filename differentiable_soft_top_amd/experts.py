@@ -402,8 +402,12 @@ def _functions():
                 if slots is None:
                     raise TypeError("the gradient of x needs the plan's slots")
                 _check_slots(x, plan)
-            y, z = experts_forward(x, w, plan, bias, act, residual, want_z=True)
-            ctx.save_for_backward(x, w, z, offsets, rows, slots)
+            if any(ctx.needs_input_grad[:3]):
+                y, z = experts_forward(x, w, plan, bias, act, residual, want_z=True)
+                ctx.save_for_backward(x, w, z, offsets, rows, slots)
+            else:  # the residual's gradient needs the offsets alone
+                y = experts_forward(x, w, plan, bias, act, residual)
+                ctx.save_for_backward(None, None, None, offsets, None, None)
             ctx.act = ACTS[act]
             ctx.set_materialize_grads(False)
             return y

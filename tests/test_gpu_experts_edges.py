@@ -478,3 +478,28 @@ def test_product_of_more_rows_than_31_bits_of_elements(dev):
     within(db, *want_db, "db")
     del x, dy, dx
     torch.cuda.empty_cache()
+
+
+# ---- what the forward keeps --------------------------------------------------------
+
+def test_product_keeps_no_z_for_a_residual_alone(dev):
+    x, w, offsets, rows, slots, b, res, dy = base.product_inputs(4000, 2, 4, 64, 512, "silu", "bf16", True, True, True,
+                                                                 0.1)
+    plan = stk.Dispatch(offsets.to(dev), rows.to(dev), slots.to(dev))
+    x, w, b, res = (t.to(dev) for t in (x, w, b, res))
+    leaf = res.requires_grad_(True)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    y = stk.experts_product(x, w, plan, bias=b, act="silu", residual=leaf)
+    held = torch.cuda.memory_allocated() - before
+    assert held < y.numel() * y.element_size() + (1 << 20)  # y alone: z would be twice its size
+    (grad,) = torch.autograd.grad(y, [leaf], dy.to(dev))
+    assert torch.equal(grad.cpu(), residual_gradient(dy, offsets))
+    # any other leaf keeps it
+    for i, t in enumerate((x, w, b)):
+        t.requires_grad_(True)
+        y = stk.experts_product(x, w, plan, bias=b, act="silu", residual=leaf)
+        (grad,) = torch.autograd.grad(y, [t], dy.to(dev))
+        t.requires_grad_(False)
+        want = ref.product(x.cpu(), w.cpu(), offsets, rows, b.cpu(), "silu", res.detach().cpu(), dy)[1 + i]
+        within(grad, *want, "leaf %d" % i)
