@@ -96,8 +96,9 @@ __global__ __launch_bounds__(kThreads) void combine_forward_kernel(CombineArgs a
     const int64_t t = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
     if (t >= a.tokens)
         return;
-    for (int n = (threadIdx.x & (lanes - 1)) * 8; n < a.N; n += lanes * 8) {
-        const int count = a.N - n;
+    // (unsigned: the step behind the last column may pass 2^31)
+    for (uint32_t n = (threadIdx.x & (lanes - 1)) * 8; n < (uint32_t)a.N; n += lanes * 8) {
+        const int count = (int)(a.N - n);
         Eight<T> add;
         add.zero();
         if (a.residual)
@@ -172,10 +173,10 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineArgs 
             w[j] = place[j] >= 0 ? a.w[t * a.k + j0 + j] : 0.0f;
             dot[j] = 0.0f;
         }
-        for (int n = own * 8; n < a.N; n += lanes * 8) {
+        for (uint32_t n = own * 8; n < (uint32_t)a.N; n += lanes * 8) {
             if (!live)
                 break;
-            const int count = a.N - n;
+            const int count = (int)(a.N - n);
             Eight<T> raw, y[kBatch];
             raw.load(a.dout, t * a.N + n, count, kWhole);
             if (a.dw) {

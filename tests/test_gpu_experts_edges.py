@@ -503,3 +503,24 @@ def test_product_keeps_no_z_for_a_residual_alone(dev):
         t.requires_grad_(False)
         want = ref.product(x.cpu(), w.cpu(), offsets, rows, b.cpu(), "silu", res.detach().cpu(), dy)[1 + i]
         within(grad, *want, "leaf %d" % i)
+
+
+def test_combine_of_a_row_of_nearly_31_bits(dev):
+    # the step behind the last of 2^31 - 8 columns passes 2^31
+    N = (1 << 31) - 8
+    y = torch.zeros(2, N, dtype=torch.bfloat16, device=dev)
+    at = torch.cat([torch.arange(40), torch.arange((1 << 30) - 20, (1 << 30) + 20), torch.arange(N - 40, N)]).to(dev)
+    small = torch.randn(2, len(at), generator=gen(67)).to(torch.bfloat16)
+    y[:, at] = small.to(dev)
+    w = torch.tensor([[0.75, 0.5]])
+    slots = torch.tensor([[1, 0]], dtype=torch.int32)
+    out = stk.combine_forward(y, w.to(dev), slots.to(dev))
+    within(out[:, at], *ref.combine(small, w, slots, None)[0], "out")
+    assert (out[0, 1000:1 << 20] == 0).all()
+    dy, dw = stk.combine_backward(out, y, w.to(dev), slots.to(dev))
+    dout = out[:, at].cpu()
+    _, want_dy, want_dw = ref.combine(small, w, slots, None, dout)
+    within(dy[:, at], *want_dy, "dy")
+    within(dw, *want_dw, "dw")
+    del y, out, dy
+    torch.cuda.empty_cache()
