@@ -12,7 +12,8 @@ library's calls one by one.  Everything is enqueued on the current stream of
 the tensors' device, without a host synchronisation, and may be captured into
 a graph.  As in the rest of the package, tensors only supply device memory and
 every step runs in the HIP library (include/soft_topk.h states each
-operator's formula).
+operator's formula).  Every operator takes one token or pair at least: an
+empty batch is refused.
 """
 from __future__ import annotations
 
