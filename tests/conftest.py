@@ -16,10 +16,10 @@ def pytest_configure(config):
 # whatever the residual holds, so it is 0 there.  test_gpu_experts_edges.py runs the same inputs against that (and
 # checks y, dx, dw and db of them as these do).
 def _wrong_residual_gradient(item):
-    if getattr(item, "originalname", "") not in ("test_product", "test_product_unaligned_storage"):
+    if item.path.name != "test_gpu_experts.py" or item.originalname not in ("test_product",
+                                                                            "test_product_unaligned_storage"):
         return False
-    values = item.callspec.params
-    return item.path.name == "test_gpu_experts.py" and values["residual"] and values["dropped"] > 0
+    return item.callspec.params["residual"] and item.callspec.params["dropped"] > 0
 
 
 def pytest_collection_modifyitems(items):
